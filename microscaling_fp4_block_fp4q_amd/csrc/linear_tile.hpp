@@ -257,9 +257,10 @@ __device__ __forceinline__ void tile_finish(const TileArgs& p, const RowTile& rt
 // 2 bytes of it, and the L2's request rate bounds the kernel.
 //
 // Past K: x is zero there, so the codes need only be finite (any code is) and
-// the scales are set to code 0.  Codes past the array's end are not read (the
-// buffer's bound); the last scale reads of the array are moved back inside
-// it and shifted.
+// the scales are set to code 0.  Codes past the array's end are not read: the
+// buffer's bound holds them back, for steps that begin inside K (the bound is
+// compared with the offset less the step's, which has to stay below it); the
+// last scale reads of the array are moved back inside it and shifted.
 template <int SF, int OF, int BO, int W>
 struct TileWeights {
     static constexpr int B = kScaleBlock<SF>;
@@ -461,7 +462,13 @@ __global__ __launch_bounds__(64 * WM * WO, PER_CU * WM * WO / 4) void k_linear_t
             const int c = min(s, ns - 1);
             x.load(st, step_of(c), plane_of(c), wave);
         };
-        const auto fetch_w = [&](uint8_t* st, int s) { wt.load(st, step_of(min(s, ns - 1)), wave); };
+        // Planes by turns go on past K to a whole group of four steps.  There x is zero
+        // and any code will do: the last step's are read, since a step's offset past the
+        // last rows of the codes is no longer one that the buffer's bound can hold back.
+        const auto fetch_w = [&](uint8_t* st, int s) {
+            const int k = step_of(min(s, ns - 1));
+            wt.load(st, TURNS == 1 ? k : min(k, (int)(p.a.K - 1) / 64), wave);
+        };
         const auto fetch_s = [&](uint64_t(&v)[OF][WT::Q], int s) { wt.load_scales(step_of(min(s, ns - 1)), v); };
         constexpr int kValu = SF == WF_E8M0 ? 2 : 6;
         // Step s = 4 n + I.  On entry oa holds substep 0 and w the step's codes; on

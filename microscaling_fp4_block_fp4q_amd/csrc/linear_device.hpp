@@ -17,6 +17,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "fp4q_device.hpp"
 
 namespace fp4q_dev {
@@ -46,6 +48,22 @@ __device__ __forceinline__ int64_t imax(int64_t a, int64_t b) { return a > b ? a
 template <class T>
 __device__ __forceinline__ T load_global(const void* p) {
     return *(const __attribute__((address_space(1))) T*)p;
+}
+
+// Work of any number of workgroups, launched in pieces: launch(first, n)
+// starts workgroups first .. first + n - 1.  HIP counts the threads of a launch
+// in 32 bits, so grids of 2^24 workgroups of 256 have to be cut.  A piece here
+// has 2^28 threads at most, which run for a millisecond and more, next to
+// which one more launch is nothing.
+template <class Launch>
+hipError_t launch_pieces(int64_t workgroups, int threads, Launch launch) {
+    const int64_t most = ((int64_t)1 << 28) / threads;
+    for (int64_t first = 0; first < workgroups; first += most) {
+        launch(first, (unsigned)std::min(most, workgroups - first));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // One product: rows of x in groups (experts), each group with its own

@@ -248,7 +248,7 @@ __device__ __forceinline__ int combine_slot(const CombineArgs& p, int64_t i) {
 template <int DT>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
     const int64_t per = (p.N + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (p.first + blockIdx.x) * 256 + threadIdx.x;
     if (i >= p.T * per) return;
     const int64_t t = i / per, c = (i - t * per) * 8;
     float sum[8] = {};
@@ -275,14 +275,14 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_combine_grad(CombineArgs p) {
     __shared__ float part[4];
     const int tid = threadIdx.x;
-    if (blockIdx.x >= p.T) {
-        const int64_t r = (int64_t)min(max(p.offsets[p.E], 0), (int)p.R) + blockIdx.x - p.T;
+    const int64_t t = p.first + blockIdx.x;
+    if (t >= p.T) {
+        const int64_t r = (int64_t)min(max(p.offsets[p.E], 0), (int)p.R) + t - p.T;
         if (r < p.R)
             for (int64_t c = 4 * tid; c < p.N; c += 1024)
                 store_y4(p.dh, p.dh_dt, r, p.ld_dh, c, p.N, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
         return;
     }
-    const int64_t t = blockIdx.x;
     for (int j = 0; j < p.top_k; ++j) {
         const int slot = combine_slot(p, t * p.top_k + j);
         const float w = p.weights ? p.weights[t * p.top_k + j] : 1.0f;
@@ -314,24 +314,26 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineArgs p) {
     }
 }
 
-hipError_t launch_combine(const CombineArgs& p, int dt, hipStream_t s) {
-    const int64_t grid = (p.T * ((p.N + 7) / 8) + 255) / 256;
-    if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid), b(256);
-    if (dt == DT_BF16) hipLaunchKernelGGL(k_combine<DT_BF16>, g, b, 0, s, p);
-    else if (dt == DT_F16) hipLaunchKernelGGL(k_combine<DT_F16>, g, b, 0, s, p);
-    else hipLaunchKernelGGL(k_combine<DT_F32>, g, b, 0, s, p);
-    return hipGetLastError();
+hipError_t launch_combine(const CombineArgs& a, int dt, hipStream_t s) {
+    return launch_pieces((a.T * ((a.N + 7) / 8) + 255) / 256, 256, [&](int64_t first, unsigned n) {
+        CombineArgs p = a;
+        p.first = first;
+        const dim3 g(n), b(256);
+        if (dt == DT_BF16) hipLaunchKernelGGL(k_combine<DT_BF16>, g, b, 0, s, p);
+        else if (dt == DT_F16) hipLaunchKernelGGL(k_combine<DT_F16>, g, b, 0, s, p);
+        else hipLaunchKernelGGL(k_combine<DT_F32>, g, b, 0, s, p);
+    });
 }
 
-hipError_t launch_combine_grad(const CombineArgs& p, int dt, hipStream_t s) {
-    const int64_t grid = p.T + p.R;
-    if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid), b(256);
-    if (dt == DT_BF16) hipLaunchKernelGGL(k_combine_grad<DT_BF16>, g, b, 0, s, p);
-    else if (dt == DT_F16) hipLaunchKernelGGL(k_combine_grad<DT_F16>, g, b, 0, s, p);
-    else hipLaunchKernelGGL(k_combine_grad<DT_F32>, g, b, 0, s, p);
-    return hipGetLastError();
+hipError_t launch_combine_grad(const CombineArgs& a, int dt, hipStream_t s) {
+    return launch_pieces(a.T + a.R, 256, [&](int64_t first, unsigned n) {
+        CombineArgs p = a;
+        p.first = first;
+        const dim3 g(n), b(256);
+        if (dt == DT_BF16) hipLaunchKernelGGL(k_combine_grad<DT_BF16>, g, b, 0, s, p);
+        else if (dt == DT_F16) hipLaunchKernelGGL(k_combine_grad<DT_F16>, g, b, 0, s, p);
+        else hipLaunchKernelGGL(k_combine_grad<DT_F32>, g, b, 0, s, p);
+    });
 }
 
 }  // namespace fp4q_dev

@@ -39,6 +39,7 @@ struct CombineArgs {
     int dh_dt;
     int64_t ld_dh;
     float* dweights;           // [T, k] or null
+    int64_t first;             // workgroup that this launch begins with
 };
 
 // Columns c .. c + 7 of a row as fp32, those at or past N zero.

@@ -127,15 +127,16 @@ struct Skinny {
 
 template <int SF, int NP, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void k_linear_skinny(LinearArgs p, int64_t plane_bytes,
-                                                                                int tiles_n) {
+                                                                                int tiles_n, int first) {
     constexpr int B = kScaleBlock<SF>;
     constexpr int U = NP * MT + NT <= 2 ? 4 : NP * MT + NT <= 5 ? 2 : 1;      // chunks in flight
     __shared__ f32x4 red[WAVES][MT * NT][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const RowTile rt = row_tile<16 * MT>(p, blockIdx.x / tiles_n);
+    const unsigned wg = (unsigned)first + blockIdx.x;
+    const RowTile rt = row_tile<16 * MT>(p, wg / tiles_n);
     if (rt.rows <= 0) return;
-    const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * (16 * NT);
+    const int64_t n0 = (int64_t)(wg % tiles_n) * (16 * NT);
     const int r = lane & 15, q = lane >> 4;
     f32x4 acc[MT][NT] = {};
     if (rt.e >= 0) {
@@ -201,9 +202,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void k_linear_skinn
 // ---------------------------------------------------------------------------
 template <int DT>
 __global__ __launch_bounds__(256) void k_linear_planes(LinearArgs p, int64_t rows, int64_t C, int64_t pitch,
-                                                       uint16_t* out) {
+                                                       uint16_t* out, int64_t first) {
     constexpr int NP = kPlanes<DT>;
-    const int64_t per = pitch / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t per = pitch / 8, i = (first + blockIdx.x) * 256 + threadIdx.x;
     if (i >= rows * per) return;
     const int64_t r = i / per, c = (i - r * per) * 8;
     u32x4 pl[NP];
@@ -214,8 +215,9 @@ __global__ __launch_bounds__(256) void k_linear_planes(LinearArgs p, int64_t row
 
 // Sum of the parts of a split product, in their order.  One lane per 4 values.
 __global__ __launch_bounds__(256) void k_linear_join(const float* part, int splits, int64_t R, int64_t O,
-                                                     int64_t ld_part, void* y, int y_dt, int64_t ld_y) {
-    const int64_t per = ld_part / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                     int64_t ld_part, void* y, int y_dt, int64_t ld_y,
+                                                     int64_t first) {
+    const int64_t per = ld_part / 4, i = (first + blockIdx.x) * 256 + threadIdx.x;
     if (i >= R * per) return;
     const int64_t r = i / per, c = (i - r * per) * 4;
     f32x4 v = *(const f32x4*)(part + r * ld_part + c);
@@ -328,9 +330,10 @@ hipError_t launch_skinny_waves(const LinearArgs& p, int64_t plane_bytes, hipStre
     const int64_t tn = (p.N + 16 * NT - 1) / (16 * NT);
     const int64_t grid = row_tiles(p.offsets != nullptr, p.R, p.E, 16 * MT) * tn;
     if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_linear_skinny<SF, NP, MT, NT, WAVES>), dim3((unsigned)grid), dim3(64 * WAVES), 0, s, p,
-                       plane_bytes, (int)tn);
-    return hipGetLastError();
+    return launch_pieces(grid, 64 * WAVES, [&](int64_t first, unsigned n) {
+        hipLaunchKernelGGL((k_linear_skinny<SF, NP, MT, NT, WAVES>), dim3(n), dim3(64 * WAVES), 0, s, p, plane_bytes,
+                           (int)tn, (int)first);
+    });
 }
 
 template <int SF, int NP, int MT, int NT>
@@ -353,32 +356,35 @@ hipError_t launch_few_rows(const LinearArgs& p, int64_t plane_bytes, hipStream_t
 
 // BIG: x gathered by 64-bit addresses.
 template <bool GRAD, int SF, int NP, bool BIG>
-hipError_t launch_tiles(const LinearPlan& q, const TileArgs& t, hipStream_t s) {
+hipError_t launch_tiles(const LinearPlan& q, const TileArgs& a, hipStream_t s) {
     const int64_t grid = q.tiles_m * q.tiles_o * q.splits;
     if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid);
-    // the small tiles take all planes of their rows together; the last argument:
-    // workgroups that a compute unit's LDS and registers hold
-    constexpr bool PI = NP > 1;
-    constexpr int TWO = NP == 3 ? 1 : 2;
-    if constexpr (GRAD) {
-        if (q.kind == Kind::kTile256)
-            hipLaunchKernelGGL((k_linear_grad_tile<SF, NP, false, 4, 2, 2, 4, 1>), g, dim3(512), 0, s, t);
-        else if (q.kind == Kind::kTile128)
-            hipLaunchKernelGGL((k_linear_grad_tile<SF, NP, false, 2, 2, 2, 2, 2>), g, dim3(256), 0, s, t);
-        else
-            hipLaunchKernelGGL((k_linear_grad_tile<SF, NP, PI, 2, 1, 1, 4, TWO>), g, dim3(256), 0, s, t);
-    } else {
-        if (q.kind == Kind::kTile256)
-            hipLaunchKernelGGL((k_linear_tile<SF, NP, false, BIG, 4, 2, 2, 4, 1>), g, dim3(512), 0, s, t);
-        else if (q.kind == Kind::kTile128)
-            hipLaunchKernelGGL((k_linear_tile<SF, NP, false, BIG, 2, 2, 2, 2, 2>), g, dim3(256), 0, s, t);
-        else if (q.kind == Kind::kTile64)
-            hipLaunchKernelGGL((k_linear_tile<SF, NP, PI, BIG, 2, 1, 1, 4, TWO>), g, dim3(256), 0, s, t);
-        else
-            hipLaunchKernelGGL((k_linear_tile<SF, NP, PI, BIG, 1, 1, 1, 4, 5 - NP>), g, dim3(256), 0, s, t);
-    }
-    return hipGetLastError();
+    return launch_pieces(grid, q.kind == Kind::kTile256 ? 512 : 256, [&](int64_t first, unsigned n) {
+        TileArgs t = a;
+        t.first = (int)first;
+        const dim3 g(n);
+        // the small tiles take all planes of their rows together; the last argument:
+        // workgroups that a compute unit's LDS and registers hold
+        constexpr bool PI = NP > 1;
+        constexpr int TWO = NP == 3 ? 1 : 2;
+        if constexpr (GRAD) {
+            if (q.kind == Kind::kTile256)
+                hipLaunchKernelGGL((k_linear_grad_tile<SF, NP, false, 4, 2, 2, 4, 1>), g, dim3(512), 0, s, t);
+            else if (q.kind == Kind::kTile128)
+                hipLaunchKernelGGL((k_linear_grad_tile<SF, NP, false, 2, 2, 2, 2, 2>), g, dim3(256), 0, s, t);
+            else
+                hipLaunchKernelGGL((k_linear_grad_tile<SF, NP, PI, 2, 1, 1, 4, TWO>), g, dim3(256), 0, s, t);
+        } else {
+            if (q.kind == Kind::kTile256)
+                hipLaunchKernelGGL((k_linear_tile<SF, NP, false, BIG, 4, 2, 2, 4, 1>), g, dim3(512), 0, s, t);
+            else if (q.kind == Kind::kTile128)
+                hipLaunchKernelGGL((k_linear_tile<SF, NP, false, BIG, 2, 2, 2, 2, 2>), g, dim3(256), 0, s, t);
+            else if (q.kind == Kind::kTile64)
+                hipLaunchKernelGGL((k_linear_tile<SF, NP, PI, BIG, 2, 1, 1, 4, TWO>), g, dim3(256), 0, s, t);
+            else
+                hipLaunchKernelGGL((k_linear_tile<SF, NP, PI, BIG, 1, 1, 1, 4, 5 - NP>), g, dim3(256), 0, s, t);
+        }
+    });
 }
 
 template <bool GRAD, int SF, int NP>
@@ -401,11 +407,10 @@ hipError_t run_product(const LinearPlan& q, const LinearArgs& p, int64_t plane_b
                                             : launch_tiles<GRAD, SF, NP, false>(q, t, s);
     else e = launch_tiles<GRAD, SF, NP, false>(q, t, s);
     if (e != hipSuccess || q.splits == 1) return e;
-    const int64_t n = (p.R * (q.ld_part / 4) + 255) / 256;
-    if (n > INT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(k_linear_join, dim3((unsigned)n), dim3(256), 0, s, t.part, q.splits, p.R,
-                       GRAD ? p.K : p.N, q.ld_part, p.y, p.y_dt, p.ld_y);
-    return hipGetLastError();
+    return launch_pieces((p.R * (q.ld_part / 4) + 255) / 256, 256, [&](int64_t first, unsigned n) {
+        hipLaunchKernelGGL(k_linear_join, dim3(n), dim3(256), 0, s, t.part, q.splits, p.R, GRAD ? p.K : p.N, q.ld_part,
+                           p.y, p.y_dt, p.ld_y, first);
+    });
 }
 
 template <bool GRAD, int SF>
@@ -438,14 +443,17 @@ hipError_t launch_linear(const LinearArgs& a, bool grad, int sf, int x_dt, void*
         const bool gather = a.rows && a.x_rows * q.pitch * 2 >= kMaxGatherBytes;
         LinearArgs from = a;
         if (!gather) from.rows = nullptr;
-        const int64_t rows = gather ? a.R : a.x_rows, n = (rows * (q.pitch / 8) + 255) / 256;
-        if (n > INT32_MAX) return hipErrorInvalidConfiguration;
-        const dim3 g((unsigned)n), b(256);
+        const int64_t rows = gather ? a.R : a.x_rows;
         uint16_t* out = (uint16_t*)workspace;
-        if (q.np == 1) hipLaunchKernelGGL(k_linear_planes<DT_BF16>, g, b, 0, s, from, rows, C, q.pitch, out);
-        else if (x_dt == DT_F16) hipLaunchKernelGGL(k_linear_planes<DT_F16>, g, b, 0, s, from, rows, C, q.pitch, out);
-        else hipLaunchKernelGGL(k_linear_planes<DT_F32>, g, b, 0, s, from, rows, C, q.pitch, out);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = launch_pieces((rows * (q.pitch / 8) + 255) / 256, 256, [&](int64_t first, unsigned n) {
+            const dim3 g(n), b(256);
+            if (q.np == 1)
+                hipLaunchKernelGGL(k_linear_planes<DT_BF16>, g, b, 0, s, from, rows, C, q.pitch, out, first);
+            else if (x_dt == DT_F16)
+                hipLaunchKernelGGL(k_linear_planes<DT_F16>, g, b, 0, s, from, rows, C, q.pitch, out, first);
+            else
+                hipLaunchKernelGGL(k_linear_planes<DT_F32>, g, b, 0, s, from, rows, C, q.pitch, out, first);
+        });
         if (e != hipSuccess) return e;
         p.x = out;
         p.ld_x = q.pitch;

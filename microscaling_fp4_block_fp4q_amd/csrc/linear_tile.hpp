@@ -93,6 +93,7 @@ struct TileArgs {
     int split_steps;           // steps of a part
     float* part;               // [splits][R][ld_part] partial sums (splits > 1)
     int64_t ld_part;
+    int first;                 // workgroup that this launch begins with
 };
 
 // The tile of workgroup id b (one part of the sum): consecutive ids go
@@ -425,9 +426,10 @@ __global__ __launch_bounds__(64 * WM * WO, PER_CU * WM * WO / 4) void k_linear_t
     __shared__ __attribute__((aligned(1024))) uint8_t wb[BO * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = 32 * MF * (wave / WO), c0 = 32 * OF * (wave % WO);
-    const int tiles = p.tiles_m * p.tiles_o, split = blockIdx.x / tiles;
+    const uint32_t wg = (uint32_t)p.first + blockIdx.x;
+    const int tiles = p.tiles_m * p.tiles_o, split = wg / tiles;
     int tm, to;
-    tile_of(p, blockIdx.x % tiles, tm, to);
+    tile_of(p, wg % tiles, tm, to);
     const RowTile rt = row_tile<BM>(p.a, tm);
     if (rt.rows <= 0) return;
     const int64_t o0 = (int64_t)to * BO;
@@ -666,9 +668,10 @@ __global__ __launch_bounds__(64 * WM * WO, PER_CU * WM * WO / 4) void k_linear_g
     __shared__ __attribute__((aligned(1024))) uint8_t ws1[64 * GW::kPitch];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = 32 * MF * (wave / WO), c0 = 32 * OF * (wave % WO);
-    const int tiles = p.tiles_m * p.tiles_o, split = blockIdx.x / tiles;
+    const uint32_t wg = (uint32_t)p.first + blockIdx.x;
+    const int tiles = p.tiles_m * p.tiles_o, split = wg / tiles;
     int tm, to;
-    tile_of(p, blockIdx.x % tiles, tm, to);
+    tile_of(p, wg % tiles, tm, to);
     const RowTile rt = row_tile<BM>(p.a, tm);
     if (rt.rows <= 0) return;
     const int64_t o0 = (int64_t)to * BO;

@@ -118,7 +118,7 @@ __device__ __forceinline__ RowTile row_tile(const LinearArgs& p, int64_t t) {
             lo = min(max(p.offsets[e], 0), R);
             hi = min(max(p.offsets[e + 1], lo), R);
         }
-        const int n = (hi - lo + BM - 1) / BM;
+        const int n = (int)(((uint32_t)(hi - lo) + (BM - 1)) / BM);     // hi - lo may be 2^31 - 1
         int incl = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {

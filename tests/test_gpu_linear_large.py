@@ -84,3 +84,9 @@ def gathered(E, edges):
 def test_experts_of_many_rows():
     note("moe_linear 2^31 - 2 rows of 3 experts")
     gathered(3, [700000001, 1500000000, (1 << 31) - 1000])
+
+
+def test_one_expert_of_almost_all_rows_that_int32_holds():
+    """Fewer than a tile below 2^31: the expert's tiles are still counted right."""
+    note("moe_linear 2^31 - 2 rows of 1 expert")
+    gathered(1, [(1 << 31) - 2])

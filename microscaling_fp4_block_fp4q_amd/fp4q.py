@@ -181,12 +181,17 @@ def _rows_cols_ld(t: torch.Tensor):
     return t.shape[0], t.shape[1], t.stride(0)
 
 
-# the current stream's handle without building a torch.cuda.Stream for it (about 2 us a call)
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# The current stream's handle without building a torch.cuda.Stream for it (about
+# 2 us a call), where torch has these: not without a GPU runtime, and they are
+# torch's own.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is None or _current_device is None:
+            return torch.cuda.current_stream().cuda_stream
         return _raw_stream(_current_device())
     return stream.cuda_stream
 

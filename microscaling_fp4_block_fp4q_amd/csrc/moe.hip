@@ -92,6 +92,15 @@ __device__ __forceinline__ void sort_count_run(const SortArgs& p, uint32_t* n, i
     for (int64_t i = i0 + lane; i < i1; i += 64) atomicAdd(&n[sort_id(p, i)], 1u);
 }
 
+// A point that the lanes of a wave pass together, with the LDS accesses of each
+// before it ahead of those of all behind it.  The LDS carries out a wave's
+// accesses in order, so this costs nothing: it keeps the compiler to it.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Place this wave's run; next[e]: places taken by earlier entries of the
 // workgroup, base[e]: first place of its expert for the workgroup.
 __device__ __forceinline__ void sort_place_run(const SortArgs& p, uint32_t* next, const uint32_t* base, int64_t i0,
@@ -102,7 +111,9 @@ __device__ __forceinline__ void sort_place_run(const SortArgs& p, uint32_t* next
         const bool in = i < i1;
         const uint32_t id = in ? sort_id(p, i) : 0u;
         const uint64_t same = same_id(id, p.id_bits) & __ballot(in);
+        wave_sync();                 // the leaders of the 64 entries before have written
         const uint32_t taken = next[id];
+        wave_sync();                 // every lane has read before a leader overwrites
         if (!in) continue;
         if ((same & below) == 0ull) next[id] = taken + (uint32_t)__popcll(same);
         const uint32_t place = base[id] + taken + (uint32_t)__popcll(same & below);

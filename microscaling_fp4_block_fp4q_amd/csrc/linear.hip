@@ -14,7 +14,7 @@
 namespace fp4q_dev {
 
 // ---------------------------------------------------------------------------
-// Few rows: 16 MT rows of x against 16 NT rows of weights per workgroup, the
+// Few rows: 16 rows of x against 16 NT rows of weights per workgroup, the
 // summed dimension K split over its waves.  Bound by the weights' bytes
 // (and for one token by latency), so weights go from memory to registers,
 // 16 bytes a lane, and are decoded there.
@@ -35,23 +35,23 @@ namespace fp4q_dev {
 // ---------------------------------------------------------------------------
 
 // A lane's part of one 128-value chunk: codes, scale codes, activations.
-template <int NP, int MT, int NT>
+template <int NP, int NT>
 struct SkinnyChunk {
     u32x4 w[NT];
     uint32_t s[NT];
-    u32x4 x[NP][MT][4];
+    u32x4 x[NP][4];
 };
 
-template <int SF, int NP, int MT, int NT>
+template <int SF, int NP, int NT>
 struct Skinny {
     const uint8_t* w[NT];      // this lane's weight rows, at its 32 values of chunk 0
     const uint8_t* s[NT];
-    const uint8_t* x[MT];      // its x rows, likewise
+    const uint8_t* x;          // its x row, likewise
     int64_t plane_bytes;
-    bool live[MT];
+    bool live;
 
     // Chunk c, all 128 values inside K.
-    __device__ __forceinline__ void load(int64_t c, SkinnyChunk<NP, MT, NT>& o) const {
+    __device__ __forceinline__ void load(int64_t c, SkinnyChunk<NP, NT>& o) const {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             o.w[j] = *(const u32x4_a8*)(w[j] + c * 64);
@@ -63,19 +63,17 @@ struct Skinny {
             }
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int q = 0; q < NP; ++q)
 #pragma unroll
-            for (int q = 0; q < NP; ++q)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    o.x[q][i][h] = u32x4{0u, 0u, 0u, 0u};
-                    if (live[i]) o.x[q][i][h] = *(const u32x4*)(x[i] + q * plane_bytes + c * 256 + 16 * h);
-                }
+            for (int h = 0; h < 4; ++h) {
+                o.x[q][h] = u32x4{0u, 0u, 0u, 0u};
+                if (live) o.x[q][h] = *(const u32x4*)(x + q * plane_bytes + c * 256 + 16 * h);
+            }
     }
 
     // The last, partial chunk: left of the lane's 32 values are inside K (a
     // multiple of 16, or none).
-    __device__ __forceinline__ void load_tail(int64_t c, int64_t left, SkinnyChunk<NP, MT, NT>& o) const {
+    __device__ __forceinline__ void load_tail(int64_t c, int64_t left, SkinnyChunk<NP, NT>& o) const {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             o.w[j] = u32x4{0u, 0u, 0u, 0u};
@@ -94,18 +92,15 @@ struct Skinny {
             }
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int q = 0; q < NP; ++q)
 #pragma unroll
-            for (int q = 0; q < NP; ++q)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    o.x[q][i][h] = u32x4{0u, 0u, 0u, 0u};
-                    if (live[i] && 8 * h < left)
-                        o.x[q][i][h] = *(const u32x4*)(x[i] + q * plane_bytes + c * 256 + 16 * h);
-                }
+            for (int h = 0; h < 4; ++h) {
+                o.x[q][h] = u32x4{0u, 0u, 0u, 0u};
+                if (live && 8 * h < left) o.x[q][h] = *(const u32x4*)(x + q * plane_bytes + c * 256 + 16 * h);
+            }
     }
 
-    static __device__ __forceinline__ void multiply(const SkinnyChunk<NP, MT, NT>& o, f32x4 (&acc)[MT][NT]) {
+    static __device__ __forceinline__ void multiply(const SkinnyChunk<NP, NT>& o, f32x4 (&acc)[NT]) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             bf16x8 a[NT];
@@ -117,33 +112,31 @@ struct Skinny {
 #pragma unroll
             for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[i][j] = mfma16<SF>(a[j], __builtin_bit_cast(bf16x8, o.x[q][i][h]), acc[i][j]);
+                for (int j = 0; j < NT; ++j)
+                    acc[j] = mfma16<SF>(a[j], __builtin_bit_cast(bf16x8, o.x[q][h]), acc[j]);
         }
     }
 };
 
-template <int SF, int NP, int MT, int NT, int WAVES>
+template <int SF, int NP, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void k_linear_skinny(LinearArgs p, int64_t plane_bytes,
                                                                                 int tiles_n, int first) {
     constexpr int B = kScaleBlock<SF>;
-    constexpr int U = NP * MT + NT <= 2 ? 4 : NP * MT + NT <= 5 ? 2 : 1;      // chunks in flight
-    __shared__ f32x4 red[WAVES][MT * NT][64];
+    constexpr int U = NP + NT <= 2 ? 4 : NP + NT <= 5 ? 2 : 1;      // chunks in flight
+    __shared__ f32x4 red[WAVES][NT][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const unsigned wg = (unsigned)first + blockIdx.x;
-    const RowTile rt = row_tile<16 * MT>(p, wg / tiles_n);
+    const RowTile rt = row_tile<16>(p, wg / tiles_n);
     if (rt.rows <= 0) return;
     const int64_t n0 = (int64_t)(wg % tiles_n) * (16 * NT);
     const int r = lane & 15, q = lane >> 4;
-    f32x4 acc[MT][NT] = {};
+    f32x4 acc[NT] = {};
     if (rt.e >= 0) {
         const int64_t K = p.K;
         const uint8_t* codes = p.codes + (int64_t)rt.e * p.N * (K / 2);
         const uint8_t* scales = p.scales + (int64_t)rt.e * p.N * (K / B);
-        Skinny<SF, NP, MT, NT> sk;
+        Skinny<SF, NP, NT> sk;
         sk.plane_bytes = plane_bytes;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -151,46 +144,39 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void k_linear_skinn
             sk.w[j] = codes + n * (K / 2) + 16 * q;
             sk.s[j] = scales + n * (K / B) + (32 / B) * q;
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int m = 16 * i + r;
-            sk.live[i] = m < rt.rows;
-            sk.x[i] = (const uint8_t*)p.x + (source_row(p, rt.row0 + (sk.live[i] ? m : 0)) * p.ld_x + 32 * q) * 2;
-        }
+        sk.live = r < rt.rows;
+        sk.x = (const uint8_t*)p.x + (source_row(p, rt.row0 + (sk.live ? r : 0)) * p.ld_x + 32 * q) * 2;
         const int64_t full = K / 128;
         int64_t c = wave;
         for (; c + (U - 1) * WAVES < full; c += U * WAVES) {
-            SkinnyChunk<NP, MT, NT> ch[U];
+            SkinnyChunk<NP, NT> ch[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) sk.load(c + u * WAVES, ch[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u) sk.multiply(ch[u], acc);
         }
         for (; c < full; c += WAVES) {
-            SkinnyChunk<NP, MT, NT> ch;
+            SkinnyChunk<NP, NT> ch;
             sk.load(c, ch);
             sk.multiply(ch, acc);
         }
         if (c == full && full * 128 < K) {
-            SkinnyChunk<NP, MT, NT> ch;
+            SkinnyChunk<NP, NT> ch;
             sk.load_tail(full, K - full * 128 - 32 * q, ch);
             sk.multiply(ch, acc);
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) red[wave][i * NT + j][lane] = acc[i][j];
+    for (int j = 0; j < NT; ++j) red[wave][j][lane] = acc[j];
     __syncthreads();
     const float g = rt.e >= 0 && p.g ? p.g[rt.e] : 1.0f;
     const float* bias = rt.e >= 0 && p.bias ? p.bias + rt.e * p.N : nullptr;
-    for (int f = wave; f < MT * NT; f += WAVES) {
+    for (int f = wave; f < NT; f += WAVES) {
         f32x4 v = red[0][f][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) v += red[w][f][lane];
-        const int m = 16 * (f / NT) + r;
-        const int64_t n = n0 + 16 * (f % NT) + 4 * q;
-        if (m < rt.rows && n < p.N) store_y4(p.y, p.y_dt, rt.row0 + m, p.ld_y, n, p.N, v * g + bias4(bias, n, p.N));
+        const int64_t n = n0 + 16 * f + 4 * q;
+        if (r < rt.rows && n < p.N) store_y4(p.y, p.y_dt, rt.row0 + r, p.ld_y, n, p.N, v * g + bias4(bias, n, p.N));
     }
 }
 
@@ -276,7 +262,7 @@ LinearPlan plan_linear(bool grad, int sf, int x_dt, bool grouped, int64_t R, int
     // (the tiles' scale reads need 8 bytes of scales)
     if (!grad && (per_group <= 16 || E * N * K < 8 * 32)) {
         q.kind = Kind::kSkinny;
-        q.copy = !as_is || C % 8 != 0;
+        q.copy = !as_is;             // (K is whole 16-byte pieces)
         if (q.copy) q.plane_bytes = round256(q.np * R * q.pitch * 2);
         return q;
     }
@@ -325,21 +311,21 @@ LinearPlan plan_linear(bool grad, int sf, int x_dt, bool grouped, int64_t R, int
     return q;
 }
 
-template <int SF, int NP, int MT, int NT, int WAVES>
+template <int SF, int NP, int NT, int WAVES>
 hipError_t launch_skinny_waves(const LinearArgs& p, int64_t plane_bytes, hipStream_t s) {
     const int64_t tn = (p.N + 16 * NT - 1) / (16 * NT);
-    const int64_t grid = row_tiles(p.offsets != nullptr, p.R, p.E, 16 * MT) * tn;
+    const int64_t grid = row_tiles(p.offsets != nullptr, p.R, p.E, 16) * tn;
     if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
     return launch_pieces(grid, 64 * WAVES, [&](int64_t first, unsigned n) {
-        hipLaunchKernelGGL((k_linear_skinny<SF, NP, MT, NT, WAVES>), dim3(n), dim3(64 * WAVES), 0, s, p, plane_bytes,
+        hipLaunchKernelGGL((k_linear_skinny<SF, NP, NT, WAVES>), dim3(n), dim3(64 * WAVES), 0, s, p, plane_bytes,
                            (int)tn, (int)first);
     });
 }
 
-template <int SF, int NP, int MT, int NT>
+template <int SF, int NP, int NT>
 hipError_t launch_skinny(const LinearArgs& p, int64_t plane_bytes, hipStream_t s) {
-    return p.offsets ? launch_skinny_waves<SF, NP, MT, NT, 4>(p, plane_bytes, s)
-                     : launch_skinny_waves<SF, NP, MT, NT, 8>(p, plane_bytes, s);
+    return p.offsets ? launch_skinny_waves<SF, NP, NT, 4>(p, plane_bytes, s)
+                     : launch_skinny_waves<SF, NP, NT, 8>(p, plane_bytes, s);
 }
 
 // The widest workgroup that still fills the device: x is read once per
@@ -349,9 +335,9 @@ hipError_t launch_skinny(const LinearArgs& p, int64_t plane_bytes, hipStream_t s
 template <int SF, int NP>
 hipError_t launch_few_rows(const LinearArgs& p, int64_t plane_bytes, hipStream_t s) {
     const int64_t n16 = (p.offsets ? std::min<int64_t>(p.E, p.R) : (p.R + 15) / 16) * ((p.N + 15) / 16);
-    if (n16 >= 4 * 224) return launch_skinny<SF, NP, 1, 4>(p, plane_bytes, s);
-    if (n16 >= 2 * 224) return launch_skinny<SF, NP, 1, 2>(p, plane_bytes, s);
-    return launch_skinny<SF, NP, 1, 1>(p, plane_bytes, s);
+    if (n16 >= 4 * 224) return launch_skinny<SF, NP, 4>(p, plane_bytes, s);
+    if (n16 >= 2 * 224) return launch_skinny<SF, NP, 2>(p, plane_bytes, s);
+    return launch_skinny<SF, NP, 1>(p, plane_bytes, s);
 }
 
 // BIG: x gathered by 64-bit addresses.

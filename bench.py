@@ -119,8 +119,8 @@ class Call:
 
 GEMM_SOURCES = ("gemm.hip",)
 # products of FP4 weights with 16/32-bit activations and the experts' routing: not on the quantize path
-OPERATOR_SOURCES = ("linear.hip", "linear.hpp", "linear_api.hip", "linear_device.hpp", "linear_tile.hpp", "moe.hip",
-                    "moe.hpp")
+OPERATOR_SOURCES = ("linear.hip", "linear.hpp", "linear_api.hip", "linear_device.hpp", "linear_plan.hpp",
+                    "linear_tile.hpp", "moe.hip", "moe.hpp")
 
 
 def source_digest(gemm: bool = False) -> str:

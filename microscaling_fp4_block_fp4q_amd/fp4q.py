@@ -766,19 +766,21 @@ def linear_grad(dy, codes, scales, cfg, g=None, out_dtype=None, workspace=None, 
 
 
 _WIDE_IDS = (torch.int64, torch.uint64, torch.uint32)
-_ID_TYPES = (torch.int32, torch.int16, torch.int8, torch.uint8, torch.uint16) + _WIDE_IDS
+_ID_TYPES = (torch.int16, torch.int8, torch.uint8, torch.uint16) + _WIDE_IDS
 
 
 def moe_sort(ids, num_experts, workspace=None, stream=None):
     """Tokens sorted by expert: ids [T, top_k] (int32; other integers are
     converted) -> dict(offsets [E+1], rows [T top_k], slots [T, top_k]), int32."""
-    if ids.dtype not in _ID_TYPES:
+    if ids.dtype is not torch.int32 and ids.dtype not in _ID_TYPES:
         raise TypeError(f"ids: expected integers, got {ids.dtype}")
     with _on(stream):
-        if ids.dtype in _WIDE_IDS:
-            ids = ids.to(torch.int64).clamp(-1, num_experts)       # any id outside stays outside
-        if ids.dtype is not torch.int32 or not ids.is_contiguous():
-            ids = ids.to(torch.int32).contiguous()
+        if ids.dtype is not torch.int32:
+            if ids.dtype in _WIDE_IDS:
+                ids = ids.to(torch.int64).clamp(-1, num_experts)   # any id outside stays outside
+            ids = ids.to(torch.int32)
+        if not ids.is_contiguous():
+            ids = ids.contiguous()
         T, top_k = ids.shape
         offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=ids.device)
         rows = torch.empty(T * top_k, dtype=torch.int32, device=ids.device)

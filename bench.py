@@ -136,6 +136,19 @@ def source_digest(gemm: bool = False) -> str:
     return h.hexdigest()[:16]
 
 
+def operator_digest() -> str:
+    """sha256 over the sources of the FP4-weight products and the experts'
+    routing without their comments and blank space (the measured figures stand
+    there): ties profiles/kernel_stats_operators.json to a kernel version."""
+    import hashlib
+    import re
+    h = hashlib.sha256()
+    for f in sorted(OPERATOR_SOURCES + ("fp4q_device.hpp",)):
+        with open(os.path.join(CSRC, f)) as fh:
+            h.update((f + " ".join(re.sub(r"//[^\n]*|/\*.*?\*/", " ", fh.read(), flags=re.S).split())).encode())
+    return h.hexdigest()[:16]
+
+
 def summarize(dirs, label, command, probe_json=None):
     """Aggregate rocprofv3 csv output (kernel stats and counter collections)
     into profiles/<label>.json (numbers) and profiles/<label>.md (table).

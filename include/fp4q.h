@@ -330,7 +330,8 @@ fp4q_status fp4q_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, con
  * weight matrix per expert, and their gradients to the activations (the
  * weights are frozen: their codes have no gradient).  With
  *   w[n][k] = fl((E2M1 value of code) * dec(scale of its block))
- * (exact, except that 4 and 6 times the largest E8M0 scales are infinities)
+ * (exact, except that a product of 2^128 and more is an infinity: 4 and 6 at
+ * E8M0 code 253, 2, 3, 4 and 6 at code 254)
  *   forward   y[m][n]  = g sum_k x[m][k] w[n][k] + bias[n]
  *   gradient  dx[m][k] = g sum_n dy[m][n] w[n][k]
  * Shared by the four calls:
@@ -349,7 +350,8 @@ fp4q_status fp4q_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, con
  *    part of one that is split, the bias is added in fp32, and the
  *    result is rounded once, half to even.  NaN scales, NaN and infinite
  *    activations propagate as in the definition; a sum that an infinite
- *    weight enters is infinite or NaN.
+ *    weight enters is infinite or NaN (with fp32 and fp16 activations NaN also
+ *    where the definition has an infinity).
  *  - A sum over no values is 0 (K = 0: y is the bias; N = 0: dx is 0).
  *  - N, K and the row stride of x / dy are at most 2^22, the rows below 2^31
  *    (FP4Q_ERR_SHAPE).

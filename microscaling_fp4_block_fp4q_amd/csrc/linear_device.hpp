@@ -2,17 +2,22 @@
 // 16- and 32-bit activations (linear.hip).
 //
 // Number formats on the matrix cores.  A weight without its per-tensor
-// scale, grid * dec(scale), has at most 2 + 4 significant bits and an
-// exponent inside bf16's range for every E8M0 and E4M3 scale, so bf16 holds
-// it exactly (the scaled convert and the matrix cores keep bf16 subnormals;
-// both were checked for every code and scale).  Activations go in as bf16
-// planes whose sum is the activation: bf16 is one plane, fp16 (11
-// significant bits) two, fp32 (24) three, each plane the next 8 bits,
-// truncated.  Every product of a plane and a weight is then exact in fp32,
-// and the fp32 accumulation is the only rounding before the result's.  An
-// E4M3-scaled weight (2^-10 .. 2688) is exact in fp16 too, so fp16
-// activations with it run on the fp16 matrix cores as they are (WF_E4M3_F16):
-// half the products of two planes.  E8M0 scales leave fp16's range.
+// scale, grid * dec(scale), has at most 2 + 4 significant bits, and its
+// exponent is inside bf16's range unless it reaches 2^128: 4 and 6 at E8M0
+// code 253 (2^126), 2, 3, 4 and 6 at code 254 (2^127), which are infinities,
+// as in fp32.  bf16 holds every other one exactly (the scaled convert and the
+// matrix cores keep bf16 subnormals; both were checked for every code and
+// scale).
+//
+// Activations go in as bf16 planes whose sum is the activation: bf16 is one
+// plane, fp16 (11 significant bits) two, fp32 (24) three, each plane the next
+// 8 bits, truncated.  Every product of a plane and a weight is then exact in
+// fp32, and the fp32 accumulation is the only rounding before the result's.
+// (With several planes an infinite weight also meets planes that are zero: the
+// sum is then NaN where the definition has an infinity.)  An E4M3-scaled
+// weight (2^-10 .. 2688) is exact in fp16 too, so fp16 activations with it run
+// on the fp16 matrix cores as they are (WF_E4M3_F16): half the products of two
+// planes.  E8M0 scales leave fp16's range.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -101,7 +101,11 @@ inline LinearPlan plan_linear(bool grad, int sf, int x_dt, bool grouped, int64_t
     q.tiles_o = (O + bo - 1) / bo;
     // Parts of the sum, by a model of the time in ns: the steps of the busiest
     // compute unit (a step of a tile takes about 200, 300, 550 and 1200 ns) and
-    // the join (4 us, and its bytes at 4 TB/s).
+    // the join (4 us, and its bytes at 4 TB/s).  It was fitted to one plane, one
+    // workgroup of a unit at a time.  Planes in one stage make a step longer than it
+    // says (17 rows fp32 at 14336 x 4096: 6.4 us predicted for a kernel of 21), and
+    // tiles of which two and more share a unit hide each other's latency, so for
+    // short products with several planes its choice is not always the best.
     const double step_ns = bm == 32 ? 200 : bm == 64 ? 300 : bm == 128 ? 550 : 1200;
     const int64_t unit = turns ? 4 : 1;
     double best = 0;

@@ -38,15 +38,19 @@
 // while the last products run.  Loads run ahead by three (forward) or two
 // (gradient) steps of activations.
 //
-// Measured (a call, with its launches): forward, 8192 x 14336 x 4096, MXFP4
-// bf16, 256 x 256 tiles 0.71-0.73 ms, 1.31-1.35 PFLOP/s; matrix cores busy
-// 0.71 of the cycles at 1.65 GHz, which is the card's power limit (a library
-// bf16 product of that shape, busy 0.89, falls to 1.48 GHz and takes 0.72-0.75
-// ms in the same run).  NVFP4 over 8 experts 0.98-1.02 ms for 8192 rows: one
-// tile in nine is padding, and decoding costs 4 instructions a pair of
-// weights against one.  Gradient, 4096 x 4096 x 14336 NVFP4, 0.44-0.46 ms,
-// 1.05-1.10 PFLOP/s: 896 tiles on 256 compute units, and LDS moves as many
-// bytes as it can while the products run.
+// Measured (a call, with its launches, over several boxes): forward, 8192 x
+// 14336 x 4096, MXFP4 bf16, 256 x 256 tiles 0.70-0.74 ms, 1.30-1.37 PFLOP/s;
+// matrix cores busy 0.71 of the cycles at 1.65 GHz, which is the card's power
+// limit (a library bf16 product of that shape, busy 0.89, falls to 1.48 GHz
+// and takes 0.72-0.75 ms in the same run).  NVFP4 over 8 experts 0.98-1.04 ms
+// for 8192 rows: one tile in nine is padding, and decoding costs 4
+// instructions a pair of weights against one, done by both wave rows (matrix
+// cores busy 0.64, VALU 0.46).  Gradient, 4096 x 4096 x 14336 NVFP4, 0.44-0.47
+// ms, 1.03-1.10 PFLOP/s: 896 tiles are 3.5 rounds of the 256 compute units and
+// take the time of four; inside a tile nothing is full (matrix cores busy
+// 0.55, VALU 0.23, LDS 0.29, of it conflicts 0.01): its waves stand in line to
+// issue for half of their time and wait at barriers and for loads for a
+// quarter.
 #pragma once
 
 #include "linear_device.hpp"

@@ -18,9 +18,11 @@ namespace fp4q_dev {
 // Atomics only count, so the table is the same on every run.
 //
 // Up to kSortSmall entries one workgroup does it all (512 entries of 64
-// experts: 3.4 us, where the three kernels took 8): launches cost more than
-// the work.  Above, three kernels (524288 entries of 256 experts: 4.6, 3.0 and
-// 9.3 us, where the 6.3 MB would take 1.3):
+// experts: 3.2-3.4 us, where the three kernels took 8): launches cost more than
+// the work.  Above, three kernels (524288 entries of 256 experts: 4.4-4.6,
+// 3.0-3.3 and 9.3 us, where the 6.3 MB would take 1.3; the last one's waves wait
+// 0.73 of their time for memory and LDS: strided counts, and a chain of
+// dependent accesses per 64 entries):
 //   k_sort_count  counts[e][c] = entries of expert e in chunk c
 //   k_sort_scan   per expert, exclusive sums over the chunks and their total
 //   k_sort_place  sums over the experts' totals, then the places
@@ -280,8 +282,11 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
 // dweights[t][j] = <h[slots[t][j]], dy[t]>; rows of dh that no entry holds
 // (from offsets[E] on) are zeros.  One workgroup per token, then per row past
 // the entries; dy[t] is read again from the cache for each of its entries.
-// Bound by bytes: 2047 tokens of 4 entries, 2056 columns, bf16, 18.6 us, 4.1
-// TB/s.
+// Bound by bytes on wide rows: 2047 tokens of 4 entries, 2056 columns, bf16,
+// 18.6 us, 4.1 TB/s; 8192 tokens of 8, 4096 columns, 248 us, 4.6 TB/s.  256
+// lanes take 2048 columns at a time and the entries one after the other, so
+// narrow rows leave lanes idle: 1024 columns 104 us (2.8 TB/s), 512 85 (1.7), 256
+// 65 (1.1).
 template <int DT>
 __global__ __launch_bounds__(256) void k_combine_grad(CombineArgs p) {
     __shared__ float part[4];

@@ -38,7 +38,7 @@
 // while the last products run.  Loads run ahead by three (forward) or two
 // (gradient) steps of activations.
 //
-// Measured (a call, with its launches, over several boxes): forward, 8192 x
+// Measured (a call, with its launches, over several runs): forward, 8192 x
 // 14336 x 4096, MXFP4 bf16, 256 x 256 tiles 0.70-0.74 ms, 1.30-1.37 PFLOP/s;
 // matrix cores busy 0.71 of the cycles at 1.65 GHz, which is the card's power
 // limit (a library bf16 product of that shape, busy 0.89, falls to 1.48 GHz
